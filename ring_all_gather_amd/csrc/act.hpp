@@ -5,6 +5,8 @@
 //              exponential factored out, so it falls off with the tail itself)
 //   gelu_tanh  z s(2 v), v = sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh v)/2 is the logistic s(2 v)
 //   silu       z s(z)
+// At z = -inf gelu, gelu_tanh and silu are NaN, as -inf * 0 in these formulas is, in the forward pass
+// and in the backward pass alike; the derivatives take their limits, 0 at -inf and 1 at +inf.
 // exp is the hardware's exp2 of x log2(e) and the reciprocal the hardware's, each good to about
 // 1 part in 2^22 here: results are rounded to bf16 (1 part in 2^8) or summed in fp32.
 #pragma once
@@ -37,9 +39,9 @@ template <int ACT>
 __device__ inline float act_value(float z) {
   if constexpr (ACT == RAG_ACT_RELU) return z < 0.0f ? 0.0f : z;
   else if constexpr (ACT == RAG_ACT_GELU) {
-    // z Phi(z) = max(z, 0) - |z| (1 - Phi(|z|)); the tail is 0 long before |z| meets its limit
     float g;
-    return (z < 0.0f ? 0.0f : z) - fminf(fabsf(z), 1e30f) * act_normal_tail(z, &g);
+    const float tail = act_normal_tail(z, &g);
+    return z * (z < 0.0f ? tail : 1.0f - tail);
   } else if constexpr (ACT == RAG_ACT_GELU_TANH)
     return z * act_logistic(1.59576912f * z * (1.0f + 0.044715f * z * z));
   else if constexpr (ACT == RAG_ACT_SILU) return z * act_logistic(z);

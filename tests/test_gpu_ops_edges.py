@@ -1,0 +1,54 @@
+"""GPU edges of the block operators: the activations at infinities, NaN and in their tails, and single
+rows.  Bounds: see ops_reference.py, or beside the test."""
+import pytest
+import torch
+
+import ops_reference as R
+from ring_all_gather_amd import binding as B
+
+from gpu_common import DEV, ctx
+from test_gpu_ops import BF16, F32, empty, gen, normal
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+
+def values(*v):
+    return torch.tensor(v, device=DEV).to(BF16)
+
+
+def forward(z, name):
+    """act(z) of a bf16 vector by fused_linear: no products, the bias alone."""
+    M = z.numel()
+    X, W = torch.zeros(1, 64, dtype=BF16, device=DEV), torch.zeros(M, 64, dtype=BF16, device=DEV)
+    Y, Z = empty(1, M), empty(1, M)
+    B.fused_linear(ctx(), X, W, Y, bias=z, act=name, Z=Z)
+    assert torch.equal(torch.nan_to_num(Z[0]), torch.nan_to_num(z))
+    return Y[0]
+
+
+def backward(z, name):
+    """(act(z), act'(z)) of a bf16 vector by gated_ffn_backward with dH = U = X = 1, T = 1: its dU
+    and dG, each rounded to bf16."""
+    F = z.numel()
+    one = torch.ones(1, F, dtype=BF16, device=DEV)
+    X, W = torch.ones(1, 64, dtype=BF16, device=DEV), torch.zeros(F, 64, dtype=BF16, device=DEV)
+    dWg, dWu = empty(F, 64), empty(F, 64)
+    B.gated_ffn_backward(ctx(), one, X, W, W, z[None], one, dWg=dWg, dWu=dWu, act=name)
+    return dWu[:, 0], dWg[:, 0]
+
+
+@pytest.mark.parametrize("name", R.ACTS)
+def test_activations_at_the_ends_of_the_range(name):
+    """Where z is infinite or huge, the value is the formula's in the forward and the backward
+    pass alike (NaN where it is -inf * 0); the slope at infinity is its limit."""
+    z = values(-INF, INF, -3e38, 3e38, -1e30, 1e30, -200.0, 200.0, 0.0, 1.0)
+    want = R.act(z.double(), name)
+    bound = R.BF * want.abs() + R.ACT_ERR[0] * want.abs() + R.ACT_ERR[1]
+    value, slope = backward(z, name)
+    R.check(forward(z, name), want, bound, "forward")
+    R.check(value, want, bound, "value in the backward pass")
+    ends = torch.ones(8, dtype=torch.float64, device=DEV)
+    if name != "none":
+        ends[::2] = 0.0
+    assert torch.equal(slope[:8].double(), ends)
