@@ -83,7 +83,8 @@ typedef enum {
 } rag_dtype;
 
 /* Activations of fused_linear and gated_ffn.  At z = -inf the last three are NaN (-inf * 0), in the
- * forward and the backward calls; derivatives take their limits there, 0 at -inf and 1 at +inf. */
+ * forward and the backward calls; derivatives take their limits there, 0 at -inf and 1 at +inf.  A
+ * NaN z gives a NaN value and a NaN derivative (RAG_ACT_NONE's derivative is 1 everywhere). */
 typedef enum {
     RAG_ACT_NONE = 0,       /* z */
     RAG_ACT_RELU = 1,       /* max(z, 0); its derivative at 0 is 0 */

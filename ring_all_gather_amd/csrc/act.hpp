@@ -6,7 +6,8 @@
 //   gelu_tanh  z s(2 v), v = sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh v)/2 is the logistic s(2 v)
 //   silu       z s(z)
 // At z = -inf gelu, gelu_tanh and silu are NaN, as -inf * 0 in these formulas is, in the forward pass
-// and in the backward pass alike; the derivatives take their limits, 0 at -inf and 1 at +inf.
+// and in the backward pass alike; the derivatives take their limits, 0 at -inf and 1 at +inf.  A NaN z
+// gives NaN in both, relu's too, so that it shows in the gradients as it does in the output.
 // exp is the hardware's exp2 of x log2(e) and the reciprocal the hardware's, each good to about
 // 1 part in 2^22 here: results are rounded to bf16 (1 part in 2^8) or summed in fp32.
 #pragma once
@@ -53,7 +54,7 @@ template <int ACT>
 __device__ inline float act_slope(float z, float* value) {
   if constexpr (ACT == RAG_ACT_RELU) {
     *value = z < 0.0f ? 0.0f : z;
-    return z > 0.0f ? 1.0f : 0.0f;
+    return z != z ? z : z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == RAG_ACT_GELU) {
     float g;
     const float tail = act_normal_tail(z, &g), c = z < 0.0f ? tail : 1.0f - tail;

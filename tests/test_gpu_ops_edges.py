@@ -52,3 +52,20 @@ def test_activations_at_the_ends_of_the_range(name):
     if name != "none":
         ends[::2] = 0.0
     assert torch.equal(slope[:8].double(), ends)
+
+
+@pytest.mark.parametrize("name", R.ACTS)
+def test_nan_stays_nan(name):
+    """A NaN pre-activation gives NaN, in the value and in every gradient that passes through it."""
+    z = values(NAN, 1.0, -1.0)
+    assert forward(z, name).isnan().tolist() == [True, False, False]
+    value, slope = backward(z, name)
+    assert value.isnan().tolist() == [True, False, False]
+    if name == "none":
+        return   # its slope does not read z
+    assert slope.isnan().tolist() == [True, False, False]
+    X, W = torch.ones(1, 64, dtype=BF16, device=DEV), torch.ones(3, 64, dtype=BF16, device=DEV)
+    dY, dW, db = torch.ones(1, 3, dtype=BF16, device=DEV), empty(3, 64), empty(3, dtype=F32)
+    B.fused_linear_backward(ctx(), dY, X, W, dW=dW, dbias=db, act=name, Z=z[None])
+    assert db.isnan().tolist() == [True, False, False]
+    assert dW.isnan().all(1).tolist() == [True, False, False]
