@@ -469,7 +469,8 @@ RAG_API int rag_rs_kernel_name(rag_ctx* ctx, int nc, int Mo, int tp, char* buf, 
  *     of their elements; everything else 16 bytes.
  *   - Outputs must not overlap inputs or each other, except Y == residual with ldr == M (the
  *     residual is then updated in place).
- *   - Sums, statistics and activations are fp32; each output is rounded once.  The backward
+ *   - Sums, statistics and activations are fp32 (an activation's value is good to 2^-14 of itself, also
+ *     where it is tiny); each output is rounded once.  The backward
  *     products take dZ (dG, dU) rounded to bf16, the type of their other operand; bias gradients
  *     are summed from the unrounded values.  No atomics: equal inputs give equal bits.
  *   - Optional pointers are NULL when unused; at least one output of a backward call must be given.

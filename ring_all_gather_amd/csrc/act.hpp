@@ -1,15 +1,19 @@
 // Activations and their derivatives in fp32, for the epilogues and the gradient kernel.
 //   relu       max(z, 0)
-//   gelu       z Phi(z), Phi the normal distribution function; its tail from Abramowitz and Stegun,
-//              Handbook of Mathematical Functions, 7.1.26 (|error| <= 1.5e-7 of erf, with the
-//              exponential factored out, so it falls off with the tail itself)
+//   gelu       z Phi(z), Phi the normal distribution function, by its tail 1 - Phi(a) = p(t) t
+//              exp(-a^2/2), t = 1 / (1 + 0.36 a): the polynomial p (degree 6) has the least largest
+//              relative error on 0 <= a <= 14 (linear program over 1600 points in 64 bits), 8.5e-7,
+//              1.2e-6 in fp32 arithmetic; above a = 14 the tail is less than any normal fp32 number
 //   gelu_tanh  z s(2 v), v = sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh v)/2 is the logistic s(2 v)
 //   silu       z s(z)
 // At z = -inf gelu, gelu_tanh and silu are NaN, as -inf * 0 in these formulas is, in the forward pass
 // and in the backward pass alike; the derivatives take their limits, 0 at -inf and 1 at +inf.  A NaN z
 // gives NaN in both, relu's too, so that it shows in the gradients as it does in the output.
-// exp is the hardware's exp2 of x log2(e) and the reciprocal the hardware's, each good to about
-// 1 part in 2^22 here: results are rounded to bf16 (1 part in 2^8) or summed in fp32.
+// exp is the hardware's exp2 of x log2(e) and the reciprocal the hardware's, each good to about 1 part
+// in 2^22.  Rounding the exponent adds 2^-24 of |x| for each operation that makes it, so values are
+// good to a relative 2^-19 + 8 2^-24 |x|, x the exponent (z, z^2/2, 2 v): the far tails are accurate to
+// their own size (z = -12: better than 2^-14) until they leave the range of normal fp32 numbers, where they are 0.
+// Results are rounded to bf16 (1 part in 2^8) or summed in fp32.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -25,13 +29,15 @@ __device__ inline float act_logistic(float x) {
   return __builtin_amdgcn_rcpf(1.0f + act_exp(-x));
 }
 
-// 1 - Phi(|z|), and exp(-z^2/2).  (The halved coefficients, and the argument's 1/sqrt(2), are
-// folded into the constants.)
+// 1 - Phi(|z|), and exp(-z^2/2).
 __device__ inline float act_normal_tail(float z, float* gauss) {
-  const float t = __builtin_amdgcn_rcpf(1.0f + 0.231641888f * fabsf(z));
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.36f * fabsf(z));
   const float p =
-      t * (0.127414796f +
-           t * (-0.142248368f + t * (0.7107068705f + t * (-0.7265760135f + t * 0.5307027145f))));
+      t * (0.14371239f +
+           t * (0.14178240f +
+                t * (0.13966253f +
+                     t * (0.02670555f +
+                          t * (0.18073241f + t * (-0.17960902f + t * 0.04701345f))))));
   *gauss = __builtin_amdgcn_exp2f(z * z * -0.72134752f);
   return p * *gauss;
 }

@@ -69,3 +69,20 @@ def test_nan_stays_nan(name):
     B.fused_linear_backward(ctx(), dY, X, W, dW=dW, dbias=db, act=name, Z=z[None])
     assert db.isnan().tolist() == [True, False, False]
     assert dW.isnan().all(1).tolist() == [True, False, False]
+
+
+@pytest.mark.parametrize("name", ["gelu", "gelu_tanh", "silu"])
+def test_tails_of_the_activations(name):
+    """Values far below zero are good to their own size: bf16's rounding, and relative errors of
+    2^-19 of the approximations and of 8 roundings of an exponent, which grow with it."""
+    z = torch.linspace(-12.0, 0.0, 4001, device=DEV).to(BF16).unique()
+    d = z.double()
+    want = {"gelu": 0.5 * d * torch.erfc(-d / 2 ** 0.5),
+            "gelu_tanh": d * torch.sigmoid(2 * (2 / torch.pi) ** 0.5 * (d + 0.044715 * d ** 3)),
+            "silu": d * torch.sigmoid(d)}[name]
+    power = {"gelu": d * d / 2, "gelu_tanh": 1.6 * (d.abs() + 0.0448 * d.abs() ** 3),
+             "silu": d.abs()}[name]
+    bound = want.abs() * (R.BF + 1.01 * (2.0 ** -19 + 8 * R.U32 * (power + 1)))
+    normal_range = want.abs() > 2.0 ** -120   # smaller factors may be flushed to zero
+    for got in (forward(z, name), backward(z, name)[0]):
+        R.check(got[normal_range], want[normal_range], bound[normal_range], name)
