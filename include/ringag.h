@@ -461,18 +461,18 @@ RAG_API int rag_rs_kernel_name(rag_ctx* ctx, int nc, int Mo, int tp, char* buf, 
  * Conventions on top of the ones above:
  *   - T (rows, tokens) may be 0: forward calls then enqueue nothing, backward calls write zero
  *     weight gradients; [T, ..] pointers are not looked at.  T <= 2^24; M, F, K <= 2^19.
- *   - Inputs [T, ..] have a row stride ld* in elements (>= their width, columns adjacent), outputs
- *     and weights are contiguous.  GEMM operands X need rows that start at 16-byte multiples
- *     (ldx a multiple of 8 bf16 or 16 fp8 elements) of at most 4 MiB; so has fused_linear's
- *     residual at most 4 MiB to a row.
+ *   - Inputs [T, ..] have a row stride ld* in elements (>= their width, columns adjacent; not looked
+ *     at where T = 1), outputs and weights are contiguous.  GEMM operands X need rows that start at
+ *     16-byte multiples (ldx a multiple of 8 bf16 or 16 fp8 elements) of at most 4 MiB; so has
+ *     fused_linear's residual at most 4 MiB to a row.
  *   - Inputs that only pass through elementwise work (x, dy, dY, dH, residual) need the alignment
  *     of their elements; everything else 16 bytes.
- *   - Outputs must not overlap inputs or each other, except Y == residual with ldr == M (the
- *     residual is then updated in place).
- *   - Sums, statistics and activations are fp32 (an activation's value is good to 2^-14 of itself, also
- *     where it is tiny); each output is rounded once.  The backward
- *     products take dZ (dG, dU) rounded to bf16, the type of their other operand; bias gradients
- *     are summed from the unrounded values.  No atomics: equal inputs give equal bits.
+ *   - Outputs must not overlap inputs or each other, except Y == residual with ldr == M or
+ *     T = 1 (the residual is then updated in place).
+ *   - Sums, statistics and activations are fp32 (an activation's value is good to 2^-14 of itself,
+ *     also where it is tiny); each output is rounded once.  The backward products take dZ (dG, dU)
+ *     rounded to bf16, the type of their other operand; bias gradients are summed from the
+ *     unrounded values.  No atomics: equal inputs give equal bits.
  *   - Optional pointers are NULL when unused; at least one output of a backward call must be given.
  */
 

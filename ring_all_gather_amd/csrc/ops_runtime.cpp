@@ -91,26 +91,30 @@ int check_sizes(const char* fn, int T, int N, const char* nname, int K, bool fp8
   return RAG_OK;
 }
 
-// The GEMM operand X: alignment and row stride.
-int check_x(const char* fn, const void* X, long long ldx, int T, int K, int esz) {
+// The GEMM operand X: alignment and row stride.  A single row has no second one for the stride to
+// lead to: whatever it is, *ldx becomes K.
+int check_x(const char* fn, const void* X, long long* ldx, int T, int K, int esz) {
   if (T == 0) return RAG_OK;
   if (!X) return fail(RAG_EINVAL, "%s: X must not be NULL", fn);
   if (misaligned(X)) return fail(RAG_EINVAL, "%s: X must be 16-byte aligned", fn);
-  if (ldx < K || (ldx * esz) % 16 || ldx * esz > kMaxRowBytes)
+  if (T == 1) *ldx = K;
+  if (*ldx < K || *ldx > kMaxRowBytes / esz || (*ldx * esz) % 16)
     return fail(RAG_EINVAL, "%s: ldx=%lld must be >= K=%d, a multiple of %d and at most %lld", fn,
-                ldx, K, 16 / esz, kMaxRowBytes / esz);
+                *ldx, K, 16 / esz, kMaxRowBytes / esz);
   return RAG_OK;
 }
 
-// An elementwise input [T, N]: not NULL, element-aligned, row stride at least its width.
-int check_rows(const char* fn, const char* name, const char* ldname, const void* p, long long ld,
+// An elementwise input [T, N]: not NULL, element-aligned, row stride at least its width (a single
+// row's becomes that).
+int check_rows(const char* fn, const char* name, const char* ldname, const void* p, long long* ld,
                int T, int N, int esz) {
   if (T == 0) return RAG_OK;
   if (!p) return fail(RAG_EINVAL, "%s: %s must not be NULL", fn, name);
   if (reinterpret_cast<uintptr_t>(p) % esz)
     return fail(RAG_EINVAL, "%s: %s is not aligned to its elements", fn, name);
-  if (ld < N || ld > (1ll << 31))
-    return fail(RAG_EINVAL, "%s: %s=%lld must be >= %d and at most 2^31", fn, ldname, ld, N);
+  if (T == 1) *ld = N;
+  if (*ld < N || *ld > (1ll << 31))
+    return fail(RAG_EINVAL, "%s: %s=%lld must be >= %d and at most 2^31", fn, ldname, *ld, N);
   return RAG_OK;
 }
 
@@ -453,7 +457,7 @@ int layer_norm(rag_ctx* c, const void* x, long long ldx, rag_dtype x_dt, int T, 
   RAG_TRY(check_norm(fn, T, H, x_dt, y_dt, w_dt));
   if (!(eps > 0.0f)) return fail(RAG_EINVAL, "%s: eps=%g must be > 0", fn, (double)eps);
   const int ex = size_of(x_dt), ey = size_of(y_dt), ew = size_of(w_dt);
-  RAG_TRY(check_rows(fn, "x", "ldx", x, ldx, T, H, ex));
+  RAG_TRY(check_rows(fn, "x", "ldx", x, &ldx, T, H, ex));
   if (!weight || (T > 0 && !y)) return fail(RAG_EINVAL, "%s: weight and y must not be NULL", fn);
   if (misaligned(weight) || misaligned(bias))
     return fail(RAG_EINVAL, "%s: weight and bias must be 16-byte aligned", fn);
@@ -493,8 +497,8 @@ int layer_norm_backward(rag_ctx* c, const void* dy, long long lddy, rag_dtype y_
   if (!c) return fail(RAG_EINVAL, "%s: ctx is NULL", fn);
   RAG_TRY(check_norm(fn, T, H, x_dt, y_dt, w_dt));
   const int ex = size_of(x_dt), ey = size_of(y_dt), ew = size_of(w_dt);
-  RAG_TRY(check_rows(fn, "dy", "lddy", dy, lddy, T, H, ey));
-  RAG_TRY(check_rows(fn, "x", "ldx", x, ldx, T, H, ex));
+  RAG_TRY(check_rows(fn, "dy", "lddy", dy, &lddy, T, H, ey));
+  RAG_TRY(check_rows(fn, "x", "ldx", x, &ldx, T, H, ex));
   if (!weight || !dweight || (T > 0 && (!mean || !rstd || !dx)))
     return fail(RAG_EINVAL, "%s: weight, mean, rstd, dx and dweight must not be NULL", fn);
   if (misaligned(weight)) return fail(RAG_EINVAL, "%s: weight must be 16-byte aligned", fn);
@@ -557,13 +561,13 @@ int fused_linear(rag_ctx* c, const void* X, long long ldx, int T, int K, const v
   const int esz = fp8 ? 1 : 2;
   RAG_TRY(check_sizes(fn, T, M, "M", K, fp8));
   RAG_TRY(check_act(fn, act));
-  RAG_TRY(check_x(fn, X, ldx, T, K, esz));
+  RAG_TRY(check_x(fn, X, &ldx, T, K, esz));
   if (!W || (T > 0 && !Y)) return fail(RAG_EINVAL, "%s: W and Y must not be NULL", fn);
   const float* scales[] = {scale_X, scale_W};
   RAG_TRY(check_scales(fn, fp8, scales, 2));
   if (misaligned(W) || misaligned(bias))
     return fail(RAG_EINVAL, "%s: W and bias must be 16-byte aligned", fn);
-  if (residual) RAG_TRY(check_rows(fn, "residual", "ldr", residual, ldr, T, M, 2));
+  if (residual) RAG_TRY(check_rows(fn, "residual", "ldr", residual, &ldr, T, M, 2));
   if (residual && T > 0 && ldr > kMaxRowBytes / 2)   // a tile's offsets fit 32 bits
     return fail(RAG_EINVAL, "%s: ldr=%lld must be at most %lld", fn, ldr, kMaxRowBytes / 2);
   const size_t out_bytes = (size_t)T * M * 2;
@@ -604,7 +608,7 @@ int gated_ffn(rag_ctx* c, const void* X, long long ldx, int T, int K, const void
   const int esz = fp8 ? 1 : 2;
   RAG_TRY(check_sizes(fn, T, F, "F", K, fp8));
   RAG_TRY(check_act(fn, act));
-  RAG_TRY(check_x(fn, X, ldx, T, K, esz));
+  RAG_TRY(check_x(fn, X, &ldx, T, K, esz));
   if (!Wg || !Wu || (T > 0 && !H)) return fail(RAG_EINVAL, "%s: Wg, Wu and H must not be NULL", fn);
   if (T > 0 && !G != !U) return fail(RAG_EINVAL, "%s: G and U must both be given or both NULL", fn);
   const float* scales[] = {scale_X, scale_Wg, scale_Wu};
@@ -640,8 +644,8 @@ int fused_linear_backward(rag_ctx* c, const void* dY, long long lddy, int T, int
   if (!c) return fail(RAG_EINVAL, "%s: ctx is NULL", fn);
   RAG_TRY(check_sizes(fn, T, M, "M", K, false));
   RAG_TRY(check_act(fn, act));
-  RAG_TRY(check_rows(fn, "dY", "lddy", dY, lddy, T, M, 2));
-  RAG_TRY(check_x(fn, X, ldx, T, K, 2));
+  RAG_TRY(check_rows(fn, "dY", "lddy", dY, &lddy, T, M, 2));
+  RAG_TRY(check_x(fn, X, &ldx, T, K, 2));
   if (!dX && !dW && !dbias) return fail(RAG_EINVAL, "%s: no output is given", fn);
   if (!W) return fail(RAG_EINVAL, "%s: W must not be NULL", fn);
   if (act != RAG_ACT_NONE && T > 0 && !Z)
@@ -743,8 +747,8 @@ int gated_ffn_backward(rag_ctx* c, const void* dH, long long lddh, int T, int F,
   if (!c) return fail(RAG_EINVAL, "%s: ctx is NULL", fn);
   RAG_TRY(check_sizes(fn, T, F, "F", K, false));
   RAG_TRY(check_act(fn, act));
-  RAG_TRY(check_rows(fn, "dH", "lddh", dH, lddh, T, F, 2));
-  RAG_TRY(check_x(fn, X, ldx, T, K, 2));
+  RAG_TRY(check_rows(fn, "dH", "lddh", dH, &lddh, T, F, 2));
+  RAG_TRY(check_x(fn, X, &ldx, T, K, 2));
   if (!dX && !dWg && !dWu) return fail(RAG_EINVAL, "%s: no output is given", fn);
   if (!dWg != !dWu) return fail(RAG_EINVAL, "%s: dWg and dWu must both be given or both NULL", fn);
   if (!Wg || !Wu || (T > 0 && (!G || !U)))

@@ -86,3 +86,53 @@ def test_tails_of_the_activations(name):
     normal_range = want.abs() > 2.0 ** -120   # smaller factors may be flushed to zero
     for got in (forward(z, name), backward(z, name)[0]):
         R.check(got[normal_range], want[normal_range], bound[normal_range], name)
+
+
+# ------------------------------------------------------------------------------- single rows
+
+def far(t, stride):
+    """The one-row matrix t with another row stride, which no access may take into account."""
+    assert t.shape[0] == 1
+    return t.as_strided(t.shape, (stride, 1))
+
+
+@pytest.mark.parametrize("stride", [131, 1 << 24, 1 << 33])
+def test_one_row_of_any_stride(stride):
+    """A single row has no second one, so its stride is not looked at: the last token of a long
+    sequence, or a row of a matrix whose stride is no multiple of 16 bytes."""
+    g = gen(51)
+    K, N = 128, 70
+    X, W, V = normal(g, 1, K), normal(g, N, K, std=0.1), normal(g, N, K, std=0.1)
+    r, dY = normal(g, 1, N), normal(g, 1, N)
+    w, b = normal(g, K), normal(g, K)
+
+    def run(change):
+        Y, Z, H, G, U = (empty(1, N) for _ in range(5))
+        B.fused_linear(ctx(), change(X), W, Y, act="silu", residual=change(r), Z=Z)
+        B.gated_ffn(ctx(), change(X), W, V, H, G=G, U=U)
+        out = [Y, Z, H, G, U]
+        for act in ("none", "silu"):
+            dX, dW, dV, db = empty(1, K), empty(N, K), empty(N, K), empty(N, dtype=F32)
+            B.fused_linear_backward(ctx(), change(dY), change(X), W, dX=dX, dW=dW, dbias=db,
+                                    act=act, Z=None if act == "none" else Z)
+            out += [dX.clone(), dW.clone(), db]
+            B.gated_ffn_backward(ctx(), change(dY), change(X), W, V, G, U, dX=dX, dWg=dW, dWu=dV,
+                                 act=act)
+            out += [dX, dW, dV]
+        y, mean, rstd = empty(1, K), empty(1, dtype=F32), empty(1, dtype=F32)
+        B.layer_norm(ctx(), change(X), w, b, y, mean=mean, rstd=rstd)
+        dx, dw, dn = empty(1, K), empty(K, dtype=F32), empty(K, dtype=F32)
+        B.layer_norm_backward(ctx(), change(y), change(X), w, mean, rstd, dx, dw, dn)
+        return out + [y, mean, rstd, dx, dw, dn]
+
+    for got, want in zip(run(lambda t: far(t, stride)), run(lambda t: t)):
+        assert not want.isnan().any() and torch.equal(got, want)
+
+
+def test_one_row_residual_in_place():
+    g = gen(52)
+    X, W, r = normal(g, 1, 128), normal(g, 70, 128, std=0.1), normal(g, 1, 70)
+    want, Y = empty(1, 70), r.clone()
+    B.fused_linear(ctx(), X, W, want, act="silu", residual=r)
+    B.fused_linear(ctx(), X, W, Y, act="silu", residual=far(Y, 73))
+    assert torch.equal(Y, want)
