@@ -414,6 +414,8 @@ def _flat(t: Optional[torch.Tensor], name: str, shape, dtypes):
 def _matrix(t: torch.Tensor, name: str):
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    if max(t.shape) >= 1 << 31:   # a 32-bit argument would take it modulo 2^32
+        raise ValueError(f"{name} must have fewer than 2^31 rows and columns, got {list(t.shape)}")
     return t.shape
 
 
