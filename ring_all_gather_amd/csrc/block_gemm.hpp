@@ -501,10 +501,10 @@ __device__ inline void epi_store(const float (&v)[8], const EpiMatrix<ALIGNED>& 
     const f32x2 p = {v[2 * c], v[2 * c + 1]};
     o[c] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
   }
-  const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
   if constexpr (ALIGNED) {
+    const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
     const int at = (l.row + step) * m.ld + l.col;
-    if (f32) {   // (a gradient's width is a multiple of 64)
+    if (f32) {   // (gradients only, whose width is a multiple of 64, so they are aligned)
       const int off = l.has_col(0) ? at * 4 : (int)kOOB;
       __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, lo), m.r, off, 0, 2);
       __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, hi), m.r, off + 16, 0, 2);
@@ -523,13 +523,7 @@ __device__ inline void epi_store(const float (&v)[8], const EpiMatrix<ALIGNED>& 
     }
   } else {
     if (!l.full() || !l.has(step)) return;
-    if (f32) {
-      char* q = m.p + (long long)step * m.ld * 4;
-      *(f32x4_u*)q = lo;
-      *(f32x4_u*)(q + 16) = hi;
-    } else {
-      *(u32x4_u*)(m.p + (long long)step * m.ld * 2) = o;
-    }
+    *(u32x4_u*)(m.p + (long long)step * m.ld * 2) = o;
   }
 }
 
@@ -709,9 +703,11 @@ __device__ __forceinline__ void block_gemm_tile(const GemmArgs& a, const TileAt&
     return;
   }
   const Epilogue ep(a.e, t.batch);
-  constexpr bool kPlain = kXS || kYS;
-  if (ep.aligned) epilogue_rows<S, MB, kGated, kPlain, true>(acc, lds, wave, lane, ep, wrow, wcol);
-  else epilogue_rows<S, MB, kGated, kPlain, false>(acc, lds, wave, lane, ep, wrow, wcol);
+  constexpr bool kPlain = kXS || kYS;   // gradients: contiguous, K (a multiple of 64) wide
+  if (kPlain || ep.aligned)
+    epilogue_rows<S, MB, kGated, kPlain, true>(acc, lds, wave, lane, ep, wrow, wcol);
+  else if constexpr (!kPlain)
+    epilogue_rows<S, MB, kGated, false, false>(acc, lds, wave, lane, ep, wrow, wcol);
 }
 
 // S: the tile; H: its half (or S again where a launch has none).

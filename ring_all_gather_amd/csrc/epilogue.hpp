@@ -13,7 +13,6 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 // row lengths cost the crossed lines and no more.
 typedef __bf16 bf16x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef __bf16 bf16x8_u __attribute__((ext_vector_type(8), aligned(2)));
-typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 
 __device__ inline f32x4 to_f32(const bf16x4& v) { return __builtin_convertvector(v, f32x4); }
 __device__ inline bf16x4 to_bf16(const f32x4& v) { return __builtin_convertvector(v, bf16x4); }
@@ -43,15 +42,9 @@ __device__ inline void store4(void* p, long long ld, int r, int c, int cols, con
   for (int k = 0; k < 4; ++k)
     if (c + k < cols) q[k] = o[k];
 }
-__device__ inline void store4_f32(void* p, long long ld, int r, int c, int cols, const f32x4& v) {
-  float* q = (float*)p + (size_t)r * ld + c;
-  if (c + 4 <= cols) {
-    *(f32x4_u*)q = v;
-    return;
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (c + k < cols) q[k] = v[k];
+// (fp32 outputs are weight gradients, K wide: all four columns are inside)
+__device__ inline void store4_f32(void* p, long long ld, int r, int c, const f32x4& v) {
+  *(f32x4*)((float*)p + (size_t)r * ld + c) = v;
 }
 
 // The epilogue of an output matrix, set up once per workgroup: uniform flags and scales.
@@ -78,7 +71,7 @@ struct Epilogue {
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = act_value<ACT>(v[k]);
     if (e.residual) v += load4(e.residual, e.ld_res, r, c, e.cols);
-    if (e.out_f32) store4_f32(out, e.ld_out, r, c, e.cols, v);
+    if (e.out_f32) store4_f32(out, e.ld_out, r, c, v);
     else store4(out, e.ld_out, r, c, e.cols, v);
   }
   template <int ACT>
