@@ -122,9 +122,18 @@ def declared_functions():
                                  flags=re.M)))
 
 
+def _fingerprint(name: str) -> str:
+    return (ctypes.c_char * 65).in_dll(lib(), f"{name}_sha256").value.decode()
+
+
 def kernels_fingerprint() -> str:
-    """SHA-256 of the gfx950 code object embedded in the loaded library."""
-    return (ctypes.c_char * 65).in_dll(lib(), "ringag_kernels_sha256").value.decode()
+    """SHA-256 of the ring kernels' gfx950 code object embedded in the loaded library."""
+    return _fingerprint("ringag_kernels")
+
+
+def ops_fingerprint() -> str:
+    """The same of the block operators' code object."""
+    return _fingerprint("ringag_ops")
 
 
 def last_error() -> str:

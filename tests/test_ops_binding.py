@@ -20,3 +20,11 @@ def test_sizes_that_do_not_fit_an_int_are_refused(rows):
                  lambda: B.gated_ffn_backward(NoContext, out, many, w, w, out, out, dX=many)):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+def test_fingerprints_of_both_code_objects():
+    """Each code object of the library has its own SHA-256, by which profiles name their build."""
+    ring, ops = B.kernels_fingerprint(), B.ops_fingerprint()
+    assert ring != ops
+    for digest in (ring, ops):
+        assert len(digest) == 64 and int(digest, 16) >= 0
