@@ -572,6 +572,22 @@ RAG_API int gated_ffn_backward(rag_ctx* ctx,
             int act, const void* G, const void* U,
             void* dX, void* dWg, void* dWu, rag_dtype dw_dt, void* stream);
 
+/* The calls whose kernels rag_ops_kernel_name reports. */
+typedef enum {
+    RAG_OP_FUSED_LINEAR = 0,
+    RAG_OP_GATED_FFN = 1,
+    RAG_OP_FUSED_LINEAR_BACKWARD = 2,   /* bf16, both products asked for */
+    RAG_OP_GATED_FFN_BACKWARD = 3
+} rag_op;
+
+/* The kernel that runs the products of a block operator of these sizes (N: M, or F of the gated
+ * ones), NUL-terminated into buf (len bytes), and for tiles its workgroups: whole tiles / half tiles /
+ * splits of K, e.g. "rag_lin_fp8_few16", "rag_ffn_bf16_t256 768/256/1" or
+ * "rag_backward_t256 dx 512/0/1 dw 768/256/1".  Diagnostics, the library's own addition, like
+ * rag_ag_kernel_name. */
+RAG_API int rag_ops_kernel_name(rag_ctx* ctx, int op, int T, int N, int K, rag_dtype dt, char* buf,
+                                int len);
+
 /* Text for the last non-zero return on the calling thread ("" if none): names the entry point,
  * the offending argument and its value, or the HIP call and its error string.  TransformerEngine
  * PR #2443, review comments: an error message should say what was chosen and what it requires

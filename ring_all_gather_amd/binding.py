@@ -30,6 +30,8 @@ RAG_BF16, RAG_FP8_E4M3, RAG_F32 = 0, 1, 2
 RAG_ACT_NONE, RAG_ACT_RELU, RAG_ACT_GELU, RAG_ACT_GELU_TANH, RAG_ACT_SILU = 0, 1, 2, 3, 4
 ACTIVATIONS = {"none": RAG_ACT_NONE, "relu": RAG_ACT_RELU, "gelu": RAG_ACT_GELU,
                "gelu_tanh": RAG_ACT_GELU_TANH, "silu": RAG_ACT_SILU}
+OPERATORS = {"fused_linear": 0, "gated_ffn": 1, "fused_linear_backward": 2,
+             "gated_ffn_backward": 3}
 RAG_STAGED_OUT, RAG_NO_COPY, RAG_COPY_ONLY, RAG_PER_CHUNK, RAG_RS_ARRIVE = 1, 2, 4, 8, 16
 RAG_OPT_COPY_ENGINE, RAG_OPT_COMM_WGS, RAG_OPT_SPIN_LIMIT_US = 1, 2, 3
 RAG_OPT_ARRIVAL_DELAY_US, RAG_OPT_WITHHOLD_MASK, RAG_OPT_TIMING, RAG_OPT_TILE = 4, 5, 6, 7
@@ -100,6 +102,7 @@ def lib():
     L.rag_kernel_times.argtypes = [vp, ctypes.POINTER(ctypes.c_float), i]
     L.rag_ag_kernel_name.argtypes = [vp, i, i, i, i, ctypes.c_char_p, i]
     L.rag_rs_kernel_name.argtypes = [vp, i, i, i, ctypes.c_char_p, i]
+    L.rag_ops_kernel_name.argtypes = [vp, i, i, i, i, i, ctypes.c_char_p, i]
     L.rag_last_error.restype = ctypes.c_char_p
     L.rag_version.restype = i
     for f in ("rag_create", "rag_destroy", "rag_set_option", "ag_gemm", "ag_gemm_ex", "gemm_rs",
@@ -107,7 +110,8 @@ def lib():
               "linear_allreduce", "layer_norm", "layer_norm_backward", "fused_linear",
               "fused_linear_backward", "gated_ffn", "gated_ffn_backward",
               "rag_check",
-              "rag_kernel_times", "rag_ag_kernel_name", "rag_rs_kernel_name"):
+              "rag_kernel_times", "rag_ag_kernel_name", "rag_rs_kernel_name",
+              "rag_ops_kernel_name"):
         getattr(L, f).restype = i
     _lib = L
     return L
@@ -207,6 +211,16 @@ class Context:
         """Entry point gemm_rs would launch for these sizes (diagnostics)."""
         buf = ctypes.create_string_buffer(128)
         _check(lib().rag_rs_kernel_name(self.h, nc, Mo, tp, buf, 128))
+        return buf.value.decode()
+
+    def ops_kernel_name(self, op: str, T: int, N: int, K: int, fp8: bool = False) -> str:
+        """Kernel that runs the products of the block operator `op` (a function's name) for these
+        sizes, with its workgroups: whole / half tiles / splits of K (diagnostics)."""
+        if op not in OPERATORS:
+            raise ValueError(f"unknown operator {op!r}: one of {sorted(OPERATORS)}")
+        buf = ctypes.create_string_buffer(128)
+        _check(lib().rag_ops_kernel_name(self.h, OPERATORS[op], T, N, K,
+                                         RAG_FP8_E4M3 if fp8 else RAG_BF16, buf, 128))
         return buf.value.decode()
 
     def check(self):

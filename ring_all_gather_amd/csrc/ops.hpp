@@ -126,6 +126,10 @@ enum OpsNormForm { kNorm0 = 0, kNorm1, kNorm2, kNorm4, kNormForms };
 // Rows: whole 4-byte words, the same streamed past the caches (not kNorm0), odd bf16 ones.
 enum OpsNormRows { kRowsWords = 0, kRowsStream, kRowsOdd, kNormRows };
 
+// Names of the products' entry points, written to buf.
+const char* ops_gemm_name(int kind, int tile, char* buf, size_t len);
+const char* ops_few_name(bool gated, bool fp8, int form, char* buf, size_t len);
+
 hipError_t load_ops_kernels(int device);
 hipError_t launch_ops_gemm(int device, int kind, int tile, const GemmArgs& a, hipStream_t s);
 hipError_t launch_backward_gemm(int device, int tile, const BackwardArgs& a, hipStream_t s);

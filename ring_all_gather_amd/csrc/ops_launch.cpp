@@ -49,6 +49,17 @@ hipError_t launch(hipFunction_t f, dim3 grid, int threads, const A& a, hipStream
 
 }  // namespace
 
+const char* ops_gemm_name(int kind, int tile, char* buf, size_t len) {
+  snprintf(buf, len, "%s_%s", kGemmName[kind],
+           tile == kOps256 ? "t256" : tile == kOps128 ? "t128" : "t128d");
+  return buf;
+}
+
+const char* ops_few_name(bool gated, bool fp8, int form, char* buf, size_t len) {
+  snprintf(buf, len, "rag_%s_%s_%s", gated ? "ffn" : "lin", fp8 ? "fp8" : "bf16", kFewName[form]);
+  return buf;
+}
+
 hipError_t load_ops_kernels(int device) {
   if (device < 0 || device >= kMaxDevices) return hipErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(g_ops_mu);
@@ -62,15 +73,13 @@ hipError_t load_ops_kernels(int device) {
   auto get = [&](hipFunction_t* f) { return hipModuleGetFunction(f, m, name); };
   for (int k = 0; k < kOpsGemms; ++k)
     for (int t = 0; t < kOpsTiles; ++t) {
-      snprintf(name, sizeof name, "%s_%s", kGemmName[k],
-               t == kOps256 ? "t256" : t == kOps128 ? "t128" : "t128d");
+      ops_gemm_name(k, t, name, sizeof name);
       if ((e = get(&d.gemm[k][t])) != hipSuccess) return e;
     }
   for (int g = 0; g < 2; ++g)
     for (int f = 0; f < 2; ++f)
       for (int t = 0; t < kFewForms; ++t) {
-        snprintf(name, sizeof name, "rag_%s_%s_%s", g ? "ffn" : "lin", f ? "fp8" : "bf16",
-                 kFewName[t]);
+        ops_few_name(g, f, t, name, sizeof name);
         if ((e = get(&d.few[g][f][t])) != hipSuccess) return e;
       }
   for (int b = 0; b < 2; ++b)

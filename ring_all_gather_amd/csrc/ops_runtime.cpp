@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdio>
 
 #include "context.hpp"
 #include "ops.hpp"
@@ -308,14 +309,43 @@ int run_backward(rag_ctx* c, const Plan& p, const Shape& sx, const Shape& sw, Ge
 
 constexpr long long kSmallWeight = 16 << 20;   // bytes
 
-int forward_product(rag_ctx* c, bool gated, bool fp8, const void* X, long long ldx, int T, int K,
-                    const void* const* W, const EpiArgs& e, hipStream_t stream) {
-  const int esz = fp8 ? 1 : 2;
+// The form for few rows that a forward product takes, or -1 for tiles.
+int few_form(const rag_ctx* c, bool gated, bool fp8, int T, int N, int K) {
   // Few rows stream the weight (8192 x 8192 bf16: 16 rows 33 us against 40 on tiles, 32 rows 51
   // against 41), up to 32 of them where the weight is small and tiles leave most of the chip idle
   // (2048 x 2048: 8.3 us against 11.8).
-  const long long w_bytes = (long long)e.cols * K * esz * (gated ? 2 : 1);
-  if (T <= 16 || (T <= 32 && w_bytes <= kSmallWeight)) {
+  const long long w_bytes = (long long)N * K * (fp8 ? 1 : 2) * (gated ? 2 : 1);
+  if (T > 32 || (T > 16 && w_bytes > kSmallWeight)) return -1;
+  // Two blocks of weight rows to a workgroup, which share the tokens' loads, where the tokens are
+  // many and one block each makes more workgroups than compute units.  16 rows, 8192 deep: 5120
+  // columns 30.5 us, shared 24.0; 4096 columns 17.6 and 23.6 (too few workgroups); 8 rows, 8192
+  // columns 30.2 and 32.6.  Gated, 8 rows: 2560 columns 25.4 and 21.4, 2048 columns 14.6 and 21.0;
+  // 4 rows, 3584 columns 25.6 and 26.5.
+  const bool twice = T > (gated ? 4 : 8) && N > (gated ? 8 : 16) * c->num_cus;
+  return T > 16 ? kFew32 : twice ? kFew16x2 : kFew16;
+}
+
+// The products of a call, by their operands' K.
+Shape forward_shape(bool gated, bool fp8, int T, int N, int K) {
+  return {T, N, 1, K * (fp8 ? 1 : 2) / 128, gated ? 2 : 1, gated};
+}
+Shape dx_shape(bool gated, int T, int N, int K) {
+  const int stages = ceil_div(N, 64);
+  return {T, K, 1, gated ? 2 * stages : stages, 1, false};
+}
+Shape dw_shape(bool gated, int T, int N, int K) {
+  return {N, K, gated ? 2 : 1, ceil_div(T, 64), gated ? 2 : 1, false};
+}
+
+int forward_kind(bool gated, bool fp8) {
+  return gated ? (fp8 ? kGemmGated8 : kGemmGated) : (fp8 ? kGemmLin8 : kGemmLin);
+}
+
+int forward_product(rag_ctx* c, bool gated, bool fp8, const void* X, long long ldx, int T, int K,
+                    const void* const* W, const EpiArgs& e, hipStream_t stream) {
+  const int esz = fp8 ? 1 : 2;
+  const int form = few_form(c, gated, fp8, T, e.cols, K);
+  if (form >= 0) {
     SkinnyArgs s = {};
     s.x = X;
     s.w[0] = W[0];
@@ -324,13 +354,6 @@ int forward_product(rag_ctx* c, bool gated, bool fp8, const void* X, long long l
     s.ldw = (long long)K * esz;
     s.kblocks = K * esz / 128;
     s.e = e;
-    // Two blocks of weight rows to a workgroup, which share the tokens' loads, where the tokens are
-    // many and one block each makes more workgroups than compute units.  16 rows, 8192 deep: 5120
-    // columns 30.5 us, shared 24.0; 4096 columns 17.6 and 23.6 (too few workgroups); 8 rows, 8192
-    // columns 30.2 and 32.6.  Gated, 8 rows: 2560 columns 25.4 and 21.4, 2048 columns 14.6 and 21.0;
-    // 4 rows, 3584 columns 25.6 and 26.5.
-    const bool twice = T > (gated ? 4 : 8) && e.cols > (gated ? 8 : 16) * c->num_cus;
-    const int form = T > 16 ? kFew32 : twice ? kFew16x2 : kFew16;
     HIPCHK(launch_skinny(c->device, gated, fp8, form, s, stream));
     return RAG_OK;
   }
@@ -342,13 +365,12 @@ int forward_product(rag_ctx* c, bool gated, bool fp8, const void* X, long long l
   a.ldy = (long long)K * esz;
   a.ksteps = a.kseg = K * esz / 128;
   a.e = e;
-  const int kind = gated ? (fp8 ? kGemmGated8 : kGemmGated) : (fp8 ? kGemmLin8 : kGemmLin);
-  const Shape shape = {T, e.cols, 1, a.ksteps, gated ? 2 : 1, gated};
+  const Shape shape = forward_shape(gated, fp8, T, e.cols, K);
   const Plan plan = plan_gemm(c, &shape, 1);
   if (plan.part_bytes[0])
     RAG_TRY(workspace(c, plan.part_bytes[0]));
   set_plan(plan, 0, shape, c->opsbuf, &a);
-  HIPCHK(launch_ops_gemm(c->device, kind, plan.tile, a, stream));
+  HIPCHK(launch_ops_gemm(c->device, forward_kind(gated, fp8), plan.tile, a, stream));
   const GemmArgs* one[] = {&a};
   return run_join(c, one, 1, gated, stream);
 }
@@ -676,8 +698,9 @@ int fused_linear_backward(rag_ctx* c, const void* dY, long long lddy, int T, int
   g.cols_pad = Mp;
   grad_shape(c, dbias != nullptr, &g);
   const int slabs = g.slabs;
-  const Shape sx = {dX ? T : 0, K, 1, Mp / 64, 1, false};
-  const Shape sw = {dW ? M : 0, K, 1, ceil_div(T, 64), 1, false};
+  Shape sx = dx_shape(false, T, M, K), sw = dw_shape(false, T, M, K);
+  if (!dX) sx.rows = 0;
+  if (!dW) sw.rows = 0;
   const Plan plan = plan_backward(c, sx, sw);
   const size_t dz_bytes = make_dz ? align_up((size_t)T * Mp * 2) : 0;
   const size_t sum_bytes = dbias ? align_up((size_t)slabs * M * 4) : 0;
@@ -768,8 +791,9 @@ int gated_ffn_backward(rag_ctx* c, const void* dH, long long lddh, int T, int F,
   RAG_TRY(check_buffers(c, fn, in, out));
   hipStream_t stream = (hipStream_t)stream_v;
   const int Fp = (F + 63) & ~63;
-  const Shape sx = {dX ? T : 0, K, 1, 2 * (Fp / 64), 1, false};
-  const Shape sw = {dWg ? F : 0, K, 2, ceil_div(T, 64), 2, false};
+  Shape sx = dx_shape(true, T, F, K), sw = dw_shape(true, T, F, K);
+  if (!dX) sx.rows = 0;
+  if (!dWg) sw.rows = 0;
   const Plan plan = plan_backward(c, sx, sw);
   // [dG | dU], a row of 2 Fp each: one K-contiguous operand of dX, two K-strided ones of dW
   const size_t dz_bytes = align_up((size_t)T * 2 * Fp * 2);
@@ -827,6 +851,38 @@ int gated_ffn_backward(rag_ctx* c, const void* dH, long long lddh, int T, int F,
   aw.e.rows = F;
   aw.e.cols = K;
   return run_backward(c, plan, sx, sw, ax, aw, parts, stream);
+}
+
+int rag_ops_kernel_name(rag_ctx* c, int op, int T, int N, int K, rag_dtype dt, char* buf, int len) {
+  const char* fn = "rag_ops_kernel_name";
+  if (!c || !buf || len < 1) return fail(RAG_EINVAL, "%s: bad arguments", fn);
+  const bool back = op == RAG_OP_FUSED_LINEAR_BACKWARD || op == RAG_OP_GATED_FFN_BACKWARD;
+  const bool gated = op == RAG_OP_GATED_FFN || op == RAG_OP_GATED_FFN_BACKWARD;
+  const bool fp8 = dt == RAG_FP8_E4M3;
+  if (op < RAG_OP_FUSED_LINEAR || op > RAG_OP_GATED_FFN_BACKWARD || T < 1 ||
+      (dt != RAG_BF16 && (!fp8 || back)))
+    return fail(RAG_EINVAL, "%s: op=%d T=%d dt=%d", fn, op, T, dt);
+  RAG_TRY(check_sizes(fn, T, N, "N", K, fp8));
+  char name[96];
+  if (back) {
+    const Plan p = plan_backward(c, dx_shape(gated, T, N, K), dw_shape(gated, T, N, K));
+    snprintf(buf, len, "%s dx %d/%d/%d dw %d/%d/%d",
+             ops_gemm_name(kGemmBackward, p.tile, name, sizeof name), p.whole[0],
+             p.blocks[0] - p.whole[0], p.splits[0], p.whole[1], p.blocks[1] - p.whole[1],
+             p.splits[1]);
+    return RAG_OK;
+  }
+  const int form = few_form(c, gated, fp8, T, N, K);
+  if (form >= 0) {
+    snprintf(buf, len, "%s", ops_few_name(gated, fp8, form, name, sizeof name));
+    return RAG_OK;
+  }
+  const Shape s = forward_shape(gated, fp8, T, N, K);
+  const Plan p = plan_gemm(c, &s, 1);
+  snprintf(buf, len, "%s %d/%d/%d",
+           ops_gemm_name(forward_kind(gated, fp8), p.tile, name, sizeof name), p.whole[0],
+           p.blocks[0] - p.whole[0], p.splits[0]);
+  return RAG_OK;
 }
 
 }  // extern "C"
