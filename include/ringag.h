@@ -461,10 +461,10 @@ RAG_API int rag_rs_kernel_name(rag_ctx* ctx, int nc, int Mo, int tp, char* buf, 
  * Conventions on top of the ones above:
  *   - T (rows, tokens) may be 0: forward calls then enqueue nothing, backward calls write zero
  *     weight gradients; [T, ..] pointers are not looked at.  T <= 2^24; M, F, K <= 2^19.
- *   - Inputs [T, ..] have a row stride ld* in elements (>= their width, columns adjacent; not looked
- *     at where T = 1), outputs and weights are contiguous.  GEMM operands X need rows that start at
- *     16-byte multiples (ldx a multiple of 8 bf16 or 16 fp8 elements) of at most 4 MiB; so has
- *     fused_linear's residual at most 4 MiB to a row.
+ *   - Inputs [T, ..] have a row stride ld* in elements (>= their width, columns adjacent; not
+ *     looked at where T = 1), outputs and weights are contiguous.  GEMM operands X need rows that
+ *     start at 16-byte multiples (ldx a multiple of 8 bf16 or 16 fp8 elements) of at most 4 MiB;
+ *     so has fused_linear's residual at most 4 MiB to a row.
  *   - Inputs that only pass through elementwise work (x, dy, dY, dH, residual) need the alignment
  *     of their elements; everything else 16 bytes.
  *   - Outputs must not overlap inputs or each other, except Y == residual with ldr == M or
@@ -581,8 +581,8 @@ typedef enum {
 } rag_op;
 
 /* The kernel that runs the products of a block operator of these sizes (N: M, or F of the gated
- * ones), NUL-terminated into buf (len bytes), and for tiles its workgroups: whole tiles / half tiles /
- * splits of K, e.g. "rag_lin_fp8_few16", "rag_ffn_bf16_t256 768/256/1" or
+ * ones), NUL-terminated into buf (len bytes), and for tiles its workgroups: whole tiles / half
+ * tiles / splits of K, e.g. "rag_lin_fp8_few16", "rag_ffn_bf16_t256 768/256/1" or
  * "rag_backward_t256 dx 512/0/1 dw 768/256/1".  Diagnostics, the library's own addition, like
  * rag_ag_kernel_name. */
 RAG_API int rag_ops_kernel_name(rag_ctx* ctx, int op, int T, int N, int K, rag_dtype dt, char* buf,

@@ -51,7 +51,8 @@ def _run(cmd, what):
 
 def build_code_object(name: str, extra=()) -> str:
     co = os.path.join(BUILD_DIR, f"{name}.co")
-    _run([HIPCC, *DEVICE_FLAGS, *DEVICE_EXTRA.get(name, []), *extra, os.path.join(CSRC, DEVICE_SRCS[name]), "-o", co],
+    _run([HIPCC, *DEVICE_FLAGS, *DEVICE_EXTRA.get(name, []), *extra,
+          os.path.join(CSRC, DEVICE_SRCS[name]), "-o", co],
          f"device compile of {DEVICE_SRCS[name]}")
     return co
 

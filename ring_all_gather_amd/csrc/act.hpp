@@ -6,14 +6,15 @@
 //              1.2e-6 in fp32 arithmetic; above a = 14 the tail is less than any normal fp32 number
 //   gelu_tanh  z s(2 v), v = sqrt(2/pi) (z + 0.044715 z^3): (1 + tanh v)/2 is the logistic s(2 v)
 //   silu       z s(z)
-// At z = -inf gelu, gelu_tanh and silu are NaN, as -inf * 0 in these formulas is, in the forward pass
-// and in the backward pass alike; the derivatives take their limits, 0 at -inf and 1 at +inf.  A NaN z
-// gives NaN in both, relu's too, so that it shows in the gradients as it does in the output.
-// exp is the hardware's exp2 of x log2(e) and the reciprocal the hardware's, each good to about 1 part
-// in 2^22.  Rounding the exponent adds 2^-24 of |x| for each operation that makes it, so values are
-// good to a relative 2^-19 + 8 2^-24 |x|, x the exponent (z, z^2/2, 2 v): the far tails are accurate to
-// their own size (z = -12: better than 2^-14) until they leave the range of normal fp32 numbers, where they are 0.
-// Results are rounded to bf16 (1 part in 2^8) or summed in fp32.
+// At z = -inf gelu, gelu_tanh and silu are NaN, as -inf * 0 in these formulas is, in the forward
+// pass and in the backward pass alike; the derivatives take their limits, 0 at -inf and 1 at +inf.
+// A NaN z gives NaN in both, relu's too, so that it shows in the gradients as it does in the
+// output.
+// exp is the hardware's exp2 of x log2(e) and the reciprocal the hardware's, each good to about 1
+// part in 2^22.  Rounding the exponent adds 2^-24 of |x| for each operation that makes it, so
+// values are good to a relative 2^-19 + 8 2^-24 |x|, x the exponent (z, z^2/2, 2 v): the far tails
+// are accurate to their own size (z = -12: better than 2^-14) until they leave the range of normal
+// fp32 numbers, where they are 0.  Results are rounded to bf16 (1 part in 2^8) or summed in fp32.
 #pragma once
 
 #include <hip/hip_runtime.h>

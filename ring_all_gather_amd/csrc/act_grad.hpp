@@ -1,22 +1,27 @@
 // The elementwise half of the backward passes, and the column sums of bias and norm gradients.
 //
 // dZ = dY act'(Z) (gated: dG = dH U act'(G), dU = dH act(G)) is written once in bf16, because each
-// of the two products reads it many times, over tiles; recomputing it from dY and Z on the way into
-// a product would double that operand's loads and put the activation's slope between them and the
-// MFMAs.  Bound by memory: 8192 x 8192 (two reads, one write of 134 MB) 65 to 74 us, 5.5 to 6.2
-// TB/s; gated 4096 x 3584 (147 MB, mostly still in the last-level cache) 25 us.
+// of the two products reads it many times, over tiles; recomputing it from dY and Z on the way
+// into a product would double that operand's loads and put the activation's slope between them and
+// the MFMAs.  bf16 because that is what the MFMA takes beside the bf16 weight or input: dZ as a
+// sum of two bf16 would double the products.  It costs accuracy in dX and dW, also where dW is
+// fp32: their relative error against 64 bits is 0.0023, where products of unrounded dZ, rounded at
+// the end, have 0.0017.  The column sums take dZ before that rounding.
+//
+// Bound by memory: 8192 x 8192 (two reads, one write of 134 MB) 65 to 77 us, 5.2 to 6.2 TB/s; gated
+// 4096 x 3584 (147 MB, mostly still in the last-level cache) 25 us.
 #pragma once
 
 #include "epilogue.hpp"
 
 namespace ringag {
 
-// 8 neighbouring bf16 of row r, as one load without branches around it, so that all of a thread's are
-// in flight together: the last columns' come from the row's last 8, and tail8 moves them into place
-// (9225 x 2237: 27.4 us; with the last columns element by element 48.4).  STREAM: loaded non-temporally, for calls that
-// touch more than the last-level cache holds (linear backward of 8192 x 8192 x 1024: 290.5 us with
-// the default policy, 281.5 with this; gated backward of 1537 x 1000 x 2048, whose inputs are still
-// cached: 36.3 us with the default, 38.0).
+// 8 neighbouring bf16 of row r, as one load without branches around it, so that all of a thread's
+// are in flight together: the last columns' come from the row's last 8, and tail8 moves them into
+// place (9225 x 2237: 27.4 us; with the last columns element by element 48.4).  STREAM: loaded
+// non-temporally, for calls that touch more than the last-level cache holds (linear backward of
+// 8192 x 8192 x 1024: 290.5 us with the default policy, 281.5 with this; gated backward of 1537 x
+// 1000 x 2048, whose inputs are still cached: 36.3 us with the default, 38.0).
 template <bool STREAM>
 __device__ inline bf16x8 load8(const void* p, long long ld, int r, int c, int cols) {
   const __bf16* row = (const __bf16*)p + (size_t)r * ld;
@@ -64,7 +69,7 @@ __device__ inline void act_grad_rows(const ActGradArgs& a) {
   const int tx = threadIdx.x & (a.tx - 1), ty = threadIdx.x / a.tx, groups = 256 / a.tx;
   const int c = (blockIdx.x * a.tx + tx) * 8;
   const int r0 = (int)blockIdx.y * a.slab_rows, r1 = min(a.rows, r0 + a.slab_rows);
-  const int past = a.cols < 8 ? 0 : max(0, c + 8 - a.cols);   // columns of this thread past the last
+  const int past = a.cols < 8 ? 0 : max(0, c + 8 - a.cols);   // columns past the last one
   float sum[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
@@ -137,9 +142,10 @@ __device__ inline void act_grad_body(const ActGradArgs& a) {
 }
 
 // Sums of the columns of a [slabs][n] array: 32 columns (a 128-byte line) per workgroup, 32 row
-// groups whose sums are added in a fixed order.  A launch of its own rather than atomics, whose
-// order would change the sums from run to run; 4 to 5 us, most of it the launch and one round of
-// loads (256 slabs of 2 x 8192: 16.8 MB in 4.7 us).
+// groups whose sums are added in a fixed order.  A launch of its own: 4 to 5 us, most of it the
+// launch and one round of loads (256 slabs of 2 x 8192: 16.8 MB in 4.7 us).  Float atomics in the
+// launch before it would change the sums from run to run; an integer count by which the last
+// workgroup to arrive adds the slabs in the same order would not, and has not been measured.
 constexpr int kSumCols = 32;
 __device__ inline void colsum_body(const ColSumArgs& a) {
   __shared__ float red[32][kSumCols + 1];

@@ -12,9 +12,14 @@
 // descriptor of the row: columns past H read as zero and are not stored, without branches that
 // would make each load wait for the last.
 // Forward 16384 x 8192 bf16: 94 to 97 us, 5.5 to 5.7 TB/s (a large copy reaches 4.96).  Backward
-// 8192 x 8192 bf16: 70 us and 4.7 for the column sums, 5.4 TB/s.  One row of 8192: 3.0 us, one round
-// trip to memory and two reductions, in a call of 6.3 to 7.3.  1777 x 1001 fp32 backward: 11.9 us for
-// both launches (21 MB, much of it still cached; seven rows to a workgroup, one after the other).
+// 8192 x 8192 bf16: 70 us and 4.7 for the column sums, 5.4 TB/s.  One row of 8192: 3.0 us, one
+// round trip to memory and two reductions, in a call of 6.3 to 7.8.  1777 x 1001 fp32 backward:
+// 11.9 us for both launches (21 MB, much of it still cached; seven rows to a workgroup, one after
+// the other).  Two forms hold more than their registers: forward with four vectors keeps 3 to 6
+// values in scratch (odd rows with an fp32 weight 56) and reads them back once a row, at the rate
+// above all the same; backward of fp32 rows of more than 8192 columns 14 to 22 (odd ones up to
+// 86), stored and read back in every row, which shows: 2048 x 16384 112.6 us against 81 for its
+// bytes, where 2048 x 8192, one vector per thread and nothing in scratch, takes 46.7 against 41.
 #pragma once
 
 #include "gemm_core.hpp"
@@ -47,10 +52,10 @@ struct Row {
 };
 
 // Cache policy (the buffer instructions' nt bit) of the rows of x, dy, y and dx.  A call that
-// touches more than the last-level cache holds streams them: forward 16384 x 8192 bf16 101.2 us with
-// the default policy, 94.9 streamed; backward 8192 x 8192 79.3 and 75.5.  One whose rows another
-// kernel has just left there finds them with the default (backward 1777 x 1001 fp32 12.6 us,
-// streamed 13.4).
+// touches more than the last-level cache holds streams them: forward 16384 x 8192 bf16 101.2 us
+// with the default policy, 94.9 streamed; backward 8192 x 8192 79.3 and 75.5.  One whose rows
+// another kernel has just left there finds them with the default (backward 1777 x 1001 fp32 12.6
+// us, streamed 13.4).
 constexpr int kCached = 0, kStream = 2;
 
 // Eight elements as they lie in memory; those past the row's end are zero.

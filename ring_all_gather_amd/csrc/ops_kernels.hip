@@ -74,8 +74,8 @@ RAG_GRAD_ENTRY(rag_ffn_grad, true, false)
 RAG_GRAD_ENTRY(rag_ffn_grad_s, true, true)
 extern "C" __global__ void __launch_bounds__(1024) rag_colsum(ColSumArgs a) { colsum_body(a); }
 
-// Threads per row at most: forward 1024 (four vectors per thread: 512); backward 1024, for bf16 rows
-// 512 with two or four vectors (the only ones that have four).
+// Threads per row at most: forward 1024 (four vectors per thread: 512); backward 1024, for bf16
+// rows 512 with two or four vectors (the only ones that have four).
 template <class XT>
 constexpr int norm_bwd_threads(int nv) {
   return sizeof(XT) == 2 && nv > 1 ? 512 : 1024;

@@ -161,6 +161,9 @@ struct Plan {
 // Microseconds of one K stage (128 bytes of K per row), by tile, as measured at a full chip with
 // the tile forced: 8192 x 8192 x 8192 on 256 x 256 tiles 772 us, four rounds of 128 stages; on two
 // 128 x 128 ones per compute unit each of a pair takes 0.95 us, on one of four stages 0.50.
+// Measured on bf16; fp8 plans take the same times, a stage there being twice the products at about
+// twice the rate and the same bytes (3001 x 2500 x 8192: 64 stages of a half tile are 60 us by
+// these, 62 measured).
 constexpr double kStageUs[kOpsTiles] = {1.40, 0.95, 0.50};
 constexpr double kHalfStageUs = 0.85;        // half a 256 x 256 tile, which reads 3/4 of its bytes
 constexpr double kTileUs = 6.0;              // a workgroup's start and epilogue
@@ -392,13 +395,13 @@ void grad_shape(const rag_ctx* c, bool sums, ActGradArgs* g) {
   g->slabs = ceil_div(g->rows, g->slab_rows);
 }
 
-// Thread count, register form and grid of a norm over H columns.  Forward, few rows: as many threads
-// on a row as it has vectors, so that one round of loads covers it; else about 256, whose rows
-// follow each other in a workgroup.  8192 columns bf16: 1 row 2.97 us of GPU time with a vector per
-// thread, with four 3.63; 500 rows 5.75 and 6.45, 1000 rows 9.6 and 9.05.  16 waves per compute unit
-// (16384 rows: 96.8 us, with 12 102.9, with 24 108.3); backward, whose rows take more registers, 8
-// (16384 x 1024: 24.9 us, with 4 33.6, with 16 26.5).  `narrow`: bf16 rows; the others' vectors take
-// twice the registers, so they get more threads instead of more vectors.
+// Thread count, register form and grid of a norm over H columns.  Forward, few rows: as many
+// threads on a row as it has vectors, so that one round of loads covers it; else about 256, whose
+// rows follow each other in a workgroup.  8192 columns bf16: 1 row 2.97 us of GPU time with a
+// vector per thread, with four 3.63; 500 rows 5.75 and 6.45, 1000 rows 9.6 and 9.05.  16 waves per
+// compute unit (16384 rows: 96.8 us, with 12 102.9, with 24 108.3); backward, whose rows take more
+// registers, 8 (16384 x 1024: 24.9 us, with 4 33.6, with 16 26.5).  `narrow`: bf16 rows; the
+// others' vectors take twice the registers, so they get more threads instead of more vectors.
 void norm_shape(const rag_ctx* c, int H, int T, bool backward, bool narrow, int* form,
                 int* threads, int* grid) {
   const int need = ceil_div(H, 8);
@@ -414,13 +417,14 @@ void norm_shape(const rag_ctx* c, int H, int T, bool backward, bool narrow, int*
   *threads = nv == 0 ? 1024 : (ceil_div(need, nv) + 63) & ~63;
   const int waves = backward ? 8 : 16;   // per compute unit
   *grid = std::min(T, c->num_cus * std::max(1, waves * 64 / *threads));
-  // backward: a workgroup's rows follow each other, and every workgroup has column sums to write and
-  // to join, so that both take equally long at rows ~ sqrt(T / 32), up to eight: of 1, 2, 3, 4 and 8
-  // rows of 8192 bf16, T = 16 takes 6.6, 7.4, 8.5, 9.6, 14.0 us of GPU time, T = 143 11.8, 10.1, 10.3,
-  // 10.9, 14.8, T = 400 16.3, 15.3, 14.4, 14.2, 16.6 (4096 x 1024: eight rows 13.9 us, sixteen 18.4).
-  // Whole rounds of compute units from one on (1777 x 1001 fp32: 254 workgroups 13.6 us, 256 12.1;
-  // 3000 x 1001: 375 14.6, 512 13.5).  Up to four short rows go to one workgroup, which then writes
-  // the sums itself (calls of 4 x 8192: 8.3 us, in two launches 10.8; 8 x 8192: 11.7 and 10.8)
+  // backward: a workgroup's rows follow each other, and every workgroup has column sums to write
+  // and to join, so that both take equally long at rows ~ sqrt(T / 32), up to eight: of 1, 2, 3, 4
+  // and 8 rows of 8192 bf16, T = 16 takes 6.6, 7.4, 8.5, 9.6, 14.0 us of GPU time, T = 143 11.8,
+  // 10.1, 10.3, 10.9, 14.8, T = 400 16.3, 15.3, 14.4, 14.2, 16.6 (4096 x 1024: eight rows 13.9 us,
+  // sixteen 18.4).  Whole rounds of compute units from one on (1777 x 1001 fp32: 254 workgroups
+  // 13.6 us, 256 12.1; 3000 x 1001: 375 14.6, 512 13.5).  Up to four short rows go to one
+  // workgroup, which then writes the sums itself (calls of 4 x 8192: 8.3 us, in two launches 10.8;
+  // 8 x 8192: 11.7 and 10.8)
   if (backward && T <= 4 && need <= 1024) *grid = std::min(T, 1);
   else if (backward) {
     const int rows = std::clamp((int)std::lround(std::sqrt(T / 32.0)), 1, 8);

@@ -1,5 +1,5 @@
-"""GPU edges of the block operators: the activations at infinities, NaN and in their tails, and single
-rows.  Bounds: see ops_reference.py, or beside the test."""
+"""GPU edges of the block operators: the activations at infinities, NaN and in their tails, and
+single rows.  Bounds: see ops_reference.py, or beside the test."""
 import pytest
 import torch
 
